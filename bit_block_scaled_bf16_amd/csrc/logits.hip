@@ -23,7 +23,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2Hi = 0.693147182464599609375f;  // float32 of ln 2
 constexpr float kLn2Lo = -1.90465429995776804525e-9f;  // ln 2 - kLn2Hi
 constexpr float kMost = 1e8f;          // |s| beyond it: masked below, NaN above
-constexpr float kLeastTail = 1e-6f;    // smaller remaining teacher mass is none
+constexpr double kLeastTail = 1e-6;    // smaller remaining teacher mass is none
 // References below c z of every unmasked logit (-1e8 log2 e = -1.4427e8): of a
 // sum that has met masked logits alone (their terms must be 0), and of a
 // finished sum that met nothing (the lowest in a join).
@@ -50,6 +50,16 @@ __device__ __forceinline__ Sum join(const Sum& a, const Sum& b) {
   t.s = fa * a.s + fb * b.s;
   t.e = fa * (a.e + da * a.s) + fb * (b.e + db * b.s);
   return t;
+}
+
+// log2 of a sum's s, as a power of two and what is left of it: 6e-8 of 1, where
+// the logarithm of s itself, up to 25, is 1e-6 off.
+struct Log2 {
+  float whole, left;
+};
+
+__device__ __forceinline__ Log2 split_log2(float s) {
+  return Log2{static_cast<float>(__builtin_amdgcn_frexp_expf(s)), log2_hw(__builtin_amdgcn_frexp_mantf(s))};
 }
 
 // ln2 (r + l) for an integer r.
@@ -284,6 +294,12 @@ __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, moved<0x142, 0xA>(v, v));
   v = fmaxf(v, moved<0x143, 0xC>(v, v));
   return from_last_lane(v);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
 }
 
 // Words in LDS for one reduction over NT threads.
@@ -967,8 +983,8 @@ __global__ __launch_bounds__(NT) void token_logprobs_backward_kernel(LogitsLaunc
 struct Taught {
   float rest;     // the teacher's remaining mass
   float masses;   // its other mass
+  float over;     // masses - 1 (renormalised: 0)
   Sum members;    // the student's logits, each column once
-  float against;  // sum q (ln q - ln2 (c z - members.r)): the loss is that + masses (L - ln2 members.r)
   int bad;        // an id lies beyond the row
   int doubled;    // an id may be named twice
 };
@@ -977,6 +993,7 @@ struct Taught {
 struct __attribute__((aligned(16))) Teacher {
   int id[NVFP4_LOGITS_MAX_K];      // -1 where absent or out of range, and from k on
   float q[NVFP4_LOGITS_MAX_K];     // mass
+  float ln_q[NVFP4_LOGITS_MAX_K];
   uint8_t slot[512];               // of are_different
   Taught m;
 };
@@ -1063,12 +1080,14 @@ __device__ __forceinline__ bool are_different(Teacher& t) {
   return false;
 }
 
-// Fills t from the alternatives; kSums: members and against too. For the first
+// Fills t from the alternatives; kSums: members and ln_q too. For the first
 // wave alone; a barrier later the others may read it. Nothing here needs the
-// row's sum, so it runs while the row's first logits are on their way.
+// row's sum, so it runs while the row's first logits are on their way. What the
+// masses leave of 1 is formed in 64 bits: it may be far below float32's u, and
+// a loss near 0 consists of such differences.
 template <bool kSums>
 __device__ __forceinline__ void teach(const LogitsLaunch& a, const Alternatives& own, Teacher& t, const Scale& c) {
-  float rest = a.tail ? 1.0f : 0.0f, masses = 0.0f, against = 0.0f;
+  float rest = a.tail ? 1.0f : 0.0f, masses = 0.0f, over = 0.0f;
   Sum members = {kNoRef, 0.0f, 0.0f};
   bool bad = false, doubled = false;
   const int lane = threadIdx.x;
@@ -1087,24 +1106,36 @@ __device__ __forceinline__ void teach(const LogitsLaunch& a, const Alternatives&
     doubled = !are_different(t);
     top = wave_max(top);
     if (a.tail || top == -kInf) top = 0.0f;
-#pragma unroll
-    for (int h = 0; h < kOwn; ++h) {
-      ln_q[h] = own.a[h] - top;
-      q[h] = expf(ln_q[h]);
-      sum += q[h];
-    }
-    masses = wave_sum(sum);
     if (a.tail) {
-      rest = 1.0f - masses;
-      if (rest < kLeastTail) rest = 0.0f;
-    } else if (masses > 0.0f) {
-      const float ln_sum = logf(masses);
+      double all = 0.0;
 #pragma unroll
       for (int h = 0; h < kOwn; ++h) {
-        q[h] /= masses;
-        ln_q[h] -= ln_sum;
+        ln_q[h] = own.a[h];
+        const double e = exp(static_cast<double>(own.a[h]));
+        q[h] = static_cast<float>(e);
+        all += e;
       }
-      masses = 1.0f;
+      all = wave_sum(all);
+      masses = static_cast<float>(all);
+      over = static_cast<float>(all - 1.0);
+      rest = all > 1.0 - kLeastTail ? 0.0f : static_cast<float>(1.0 - all);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kOwn; ++h) {
+        ln_q[h] = own.a[h] - top;
+        q[h] = expf(ln_q[h]);
+        sum += q[h];
+      }
+      masses = wave_sum(sum);
+      if (masses > 0.0f) {
+        const float ln_sum = logf(masses);
+#pragma unroll
+        for (int h = 0; h < kOwn; ++h) {
+          q[h] /= masses;
+          ln_q[h] -= ln_sum;
+        }
+        masses = 1.0f;
+      }
     }
 #pragma unroll
     for (int h = 0; h < kOwn; ++h) t.q[lane + 64 * h] = q[h];
@@ -1116,26 +1147,23 @@ __device__ __forceinline__ void teach(const LogitsLaunch& a, const Alternatives&
         if (id >= 0 && !(doubled && named_before(t, id, lane + 64 * h))) add_one<false>(run, own.x[h], c);
       }
       members = wave_join(finished(run));
-      float part = 0.0f;
 #pragma unroll
-      for (int h = 0; h < kOwn; ++h)
-        if (q[h] != 0.0f)
-          part += own.x[h] <= c.low ? kInf : q[h] * (ln_q[h] - fma_(own.x[h], c.c, -members.r) * kLn2Hi);
-      against = wave_sum(part);
+      for (int h = 0; h < kOwn; ++h) t.ln_q[lane + 64 * h] = ln_q[h];
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < kOwn; ++h) t.id[lane + 64 * h] = -1;
+    for (int h = 0; h < kOwn; ++h) {
+      t.id[lane + 64 * h] = -1;
+      t.q[lane + 64 * h] = 0.0f;
+    }
   }
   if (lane == 0) {
     t.m.rest = rest;
     t.m.masses = masses;
     t.m.bad = bad;
     t.m.doubled = doubled;
-    if (kSums) {
-      t.m.members = members;
-      t.m.against = against;
-    }
+    t.m.over = over;
+    if (kSums) t.m.members = members;
   }
 }
 
@@ -1242,20 +1270,70 @@ struct RowSums {
   Sum tail, whole;
 };
 
+// q (d - 1) + p for masses q > 0 and p = q e^-d: not negative, and near d = 0,
+// where its parts cancel, from the series q (d^2/2! - d^3/3! + ...). At |d| = 1
+// the last term left out is 1e-8 of it, and the other form has 7 u.
+__device__ __forceinline__ float excess(float q, float d, float p) {
+  if (fabsf(d) > 1.0f) return fma_(q, d - 1.0f, p);
+  float g = 1.0f / 39916800.0f;  // 11!
+  g = fma_(g, -d, 1.0f / 3628800.0f);
+  g = fma_(g, -d, 1.0f / 362880.0f);
+  g = fma_(g, -d, 1.0f / 40320.0f);
+  g = fma_(g, -d, 1.0f / 5040.0f);
+  g = fma_(g, -d, 1.0f / 720.0f);
+  g = fma_(g, -d, 1.0f / 120.0f);
+  g = fma_(g, -d, 1.0f / 24.0f);
+  g = fma_(g, -d, 1.0f / 6.0f);
+  g = fma_(g, -d, 0.5f);
+  return q * (d * d * g);
+}
+
+// The row's divergence, in lane 0 of the first wave, which alone calls this. With
+// d = ln (q / p) the terms q d cancel where the student is near its teacher;
+// excess(q, d, p) = q d - q + p do not. Their sum lacks Q - P, the teacher's mass
+// on the terms less the student's. All of the student's masses together are 1,
+// so of P only what counts not once is added up: columns named without mass, or
+// twice, and the tail where it is no term.
+__device__ __forceinline__ float divergence(const Alternatives& own, const Sum& whole, const Sum& tail,
+                                            const Teacher& t, const Scale& c) {
+  const Taught& m = t.m;
+  const int lane = threadIdx.x;
+  const Log2 l = split_log2(whole.s);
+  float part = 0.0f;
+#pragma unroll
+  for (int h = 0; h < kOwn; ++h) {
+    const int j = lane + 64 * h, id = t.id[j];
+    const float q = t.q[j], y = fma_(own.x[h], c.c, -whole.r);
+    const bool live = own.x[h] > c.low;  // not so for an absent one
+    const float p = live ? exp2_hw(y) / whole.s : 0.0f;
+    const bool term = q != 0.0f, once = live && !(m.doubled && named_before(t, id, j));
+    if (term) part += excess(q, live ? t.ln_q[j] - ((y - l.whole) - l.left) * kLn2Hi : kInf, p);
+    if (term != once) part += once ? p : -p;
+  }
+  float loss = wave_sum(part);
+  const float p_rest = tail.s == 0.0f ? 0.0f : exp2_hw(shift_of(tail.r, whole.r)) * (tail.s / whole.s);
+  if (m.rest > 0.0f) {
+    const Log2 r = split_log2(tail.s);
+    const float lp = ((tail.r - whole.r) + (r.whole - l.whole)) + (r.left - l.left);
+    loss += excess(m.rest, tail.s == 0.0f ? kInf : logf(m.rest) - lp * kLn2Hi, p_rest);
+  } else if (m.masses == 0.0f) {
+    loss = 0.0f;  // a teacher without mass
+  } else {
+    loss += m.over + p_rest;
+  }
+  return loss;
+}
+
 // Joins the alternatives to the tail and writes the row's outputs.
 __device__ __forceinline__ RowSums finish_distill(const LogitsLaunch& a, int64_t at, int64_t token, float x_token,
-                                                  const Sum& tail, const Taught& m, const Scale& c) {
-  const RowSums s = {tail, a.k > 0 ? join(tail, m.members) : tail};
+                                                  const Sum& tail, const Alternatives& own, const Teacher& t,
+                                                  const Scale& c) {
+  const RowSums s = {tail, a.k > 0 ? join(tail, t.m.members) : tail};
+  float loss = 0.0f;
+  if (threadIdx.x < 64) loss = divergence(own, s.whole, tail, t, c);
   if (threadIdx.x == 0) {
     const float l2 = log2_hw(s.whole.s), tail_l2 = log2_hw(tail.s);
-    bool bad = s.whole.s != s.whole.s || m.bad;
-    float loss = 0.0f;
-    if (m.masses != 0.0f) loss = m.against + m.masses * (((s.whole.r - m.members.r) + l2) * kLn2Hi);
-    if (m.against == kInf || (m.masses != 0.0f && s.whole.s == 0.0f)) loss = kInf;
-    if (m.rest > 0.0f) {
-      const float lp = tail.s == 0.0f ? -kInf : ((tail.r - s.whole.r) + (tail_l2 - l2)) * kLn2Hi;
-      loss += m.rest * (logf(m.rest) - lp);
-    }
+    bool bad = s.whole.s != s.whole.s || t.m.bad;
     if (bad) loss = __builtin_nanf("");
     a.loss[at] = loss;
     a.lse[at] = s.whole.s == 0.0f ? -kInf : to_nats(s.whole.r, l2);
@@ -1299,7 +1377,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(LogitsLaunch a, Cut cut) {
     if (threadIdx.x == 0) part_sums(a)[blockIdx.x] = Part{t.r, t.s, 0.0f, 0.0f};
     return;
   }
-  finish_distill(a, at, token, x_token, t, teacher.m, c);
+  finish_distill(a, at, token, x_token, t, own, teacher, c);
 }
 
 // Finishes rows that were cut into parts: 4 us, most of it a launch's latency.
@@ -1315,7 +1393,7 @@ __global__ __launch_bounds__(NT) void distill_join_kernel(LogitsLaunch a, Cut cu
   const int64_t token = load_token(a, z, at, &x_token);
   if (threadIdx.x < 64) teach<true>(a, own, teacher, c);
   const Sum t = join_parts(a, at, cut, lds);  // its barriers: teacher.m is there
-  finish_distill(a, at, token, x_token, t, teacher.m, c);
+  finish_distill(a, at, token, x_token, t, own, teacher, c);
 }
 
 // Upstream gradients of a row.
@@ -1491,7 +1569,7 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
   if (single.column >= 0 && !marks.single()) add_one<false>(run, single.logit(), c);
   const Sum t = block_join(finished(run), lds);
   const Taught m = teacher.m;
-  const RowSums s = finish_distill(a, at, token, x_token, t, m, c);
+  const RowSums s = finish_distill(a, at, token, x_token, t, own, teacher, c);
   if ((g.gl == 0.0f && g.gk == 0.0f) || s.whole.s == 0.0f) {
     flat_pass<T, NT>(row, dz, in, false, c);
     return;

@@ -24,9 +24,9 @@ constexpr float kLn2Hi = 0.693147182464599609375f;  // float32 of ln 2
 constexpr float kLn2Lo = -1.90465429995776804525e-9f;  // ln 2 - kLn2Hi
 constexpr float kMost = 1e8f;          // |s| beyond it: masked below, NaN above
 constexpr double kLeastTail = 1e-6;    // smaller remaining teacher mass is none
-// References below c z of every unmasked logit (-1e8 log2 e = -1.4427e8): of a
-// sum that has met masked logits alone (their terms must be 0), and of a
-// finished sum that met nothing (the lowest in a join).
+// References: of a sum that has met masked logits alone, above the bound of their
+// c z (-1e8 log2 e = -1.442695e8) by so much that their terms are 0; and of a
+// finished sum that met nothing, below it (the lowest in a join).
 constexpr float kFirstRef = -1.4426e8f;
 constexpr float kNoRef = -2e8f;
 constexpr float kInf = __builtin_inff();
@@ -243,7 +243,8 @@ template <bool kEntropy, int n>
 __device__ __forceinline__ void add_logits(Running& a, const float (&z)[n], float top, const Scale& c) {
   if (top > a.next) {
     const float r = top > c.high ? __builtin_nanf("") : rintf(top * c.c);
-    const float d = shift_of(a.t.r, r), f = exp2_hw(d);
+    // the first unmasked logit may lie below kFirstRef: nothing has been summed then
+    const float d = fminf(shift_of(a.t.r, r), 0.0f), f = exp2_hw(d);
     a.t.e = f * (a.t.e + d * a.t.s);
     a.t.s *= f;
     a.t.r = r;

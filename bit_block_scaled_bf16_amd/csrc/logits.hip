@@ -196,6 +196,11 @@ __device__ __forceinline__ int used_of(int first, int hi) {
   return __builtin_amdgcn_readfirstlane(used < U ? used : U);
 }
 
+// The tiles of one workgroup, in vectors.
+struct Range {
+  int lo, hi;
+};
+
 // ---------------------------------------------------------------------------
 // Sums
 // ---------------------------------------------------------------------------
@@ -238,7 +243,8 @@ __device__ __forceinline__ float max_of(const float (&x)[n]) {
 // Adds logits, the largest of which is `top`. |c z| < 2^28, so r is off c z by
 // 8 at most where it is too large for a fraction; and logits up to 8 (in log2)
 // above the reference are taken as they come, which costs a sum nothing and
-// leaves the entropy's e an error of 8 u.
+// leaves the entropy's e an error of 8 u. A masked logit's term is 0 by itself
+// unless the reference is below kFirstRef (see without_masked).
 template <bool kEntropy, int n>
 __device__ __forceinline__ void add_logits(Running& a, const float (&z)[n], float top, const Scale& c) {
   if (top > a.next) {
@@ -261,8 +267,38 @@ __device__ __forceinline__ void add_logits(Running& a, const float (&z)[n], floa
 
 template <bool kEntropy>
 __device__ __forceinline__ void add_one(Running& a, float z, const Scale& c) {
-  const float one[1] = {z};
-  add_logits<kEntropy>(a, one, z, c);
+  const float one[1] = {z <= c.low ? -kInf : z};
+  add_logits<kEntropy>(a, one, one[0], c);
+}
+
+// The thread's sum over its vectors of `in` again where its reference has stayed
+// below kFirstRef: all it has met lies within 7000 of the mask's bound, and
+// masked logits may have counted. out(column): whether a column is left out too.
+// In the pass itself the comparisons, though in a branch that is hardly ever
+// taken, cost 2048 x 131072 bf16 (distillation) 86 to 93 us instead of 84.
+template <typename T, int NT, bool kEntropy, typename F>
+__device__ __forceinline__ void without_masked(Running& a, const Row<T>& row, const Range& in, const Scale& c, F out) {
+  if (!(a.t.r < kFirstRef)) return;
+  constexpr int n = Vec<T>::n;
+  a = running(c);
+#pragma unroll 1
+  for (int v = in.lo + static_cast<int>(threadIdx.x); v < in.hi; v += NT) {
+    if (!row.whole(v)) continue;
+    float x[n];
+    Vec<T>::unpack(load_vec<T, kKeep>(row.z + row.column(v)), x);
+    // as bits first: written as `if (... || out(...)) x[e] = -kInf`, clang 22 for
+    // gfx950 dropped the assignment where out() is true
+    uint32_t gone = 0;
+#pragma unroll
+    for (int e = 0; e < n; ++e) {
+      uint32_t drop = x[e] <= c.low;
+      if (!drop) drop = out(row.column(v) + e);
+      gone |= drop << e;
+    }
+#pragma unroll
+    for (int e = 0; e < n; ++e) x[e] = gone >> e & 1u ? -kInf : x[e];
+    add_logits<kEntropy>(a, x, max_of(x), c);
+  }
 }
 
 __device__ __forceinline__ Sum finished(const Running& a) {
@@ -487,11 +523,6 @@ __device__ int keep_best(Top<NT>& t, int n, int k) {
 struct Cut {
   int parts;  // workgroups a row
   int tiles;  // tiles a workgroup
-};
-
-// The tiles of one workgroup, in vectors.
-struct Range {
-  int lo, hi;
 };
 
 template <int NT, int U>
@@ -768,6 +799,7 @@ __global__ __launch_bounds__(NT) void token_logprobs_kernel(LogitsLaunch a, Cut 
       }
     }
   }
+  without_masked<T, NT, kEntropy>(run, row, in, c, [](int64_t) { return false; });
   if (edge >= 0) add_one<kEntropy>(run, x_edge, c);
   int found = 0;
   const unsigned long long* list = nullptr;
@@ -1037,6 +1069,17 @@ __device__ __forceinline__ bool named_before(const Teacher& t, int id, int j) {
     found |= four.x == id | (i + 1 < j & four.y == id) | (i + 2 < j & four.z == id) | (i + 3 < j & four.w == id);
   }
   return found;
+}
+
+// Whether the column is an alternative, k of which have been named.
+__device__ __forceinline__ bool is_named(const Teacher& t, int64_t column, int k) {
+  return named_before(t, static_cast<int>(column), k);
+}
+
+// Names the alternatives, as teach does (for the first wave).
+__device__ __forceinline__ void name(const Alternatives& own, Teacher& t) {
+#pragma unroll
+  for (int h = 0; h < kOwn; ++h) t.id[threadIdx.x + 64 * h] = own.id[h];
 }
 
 // What the first wave has written to LDS so far is there for its other lanes.
@@ -1366,11 +1409,15 @@ __global__ __launch_bounds__(NT) void distill_kernel(LogitsLaunch a, Cut cut) {
   single.load(row, in);
   Raw r[U];
   load_tile<T, NT, U, kStream>(row, in.lo, r);
-  if (cut.parts == 1 && threadIdx.x < 64) teach<true>(a, own, teacher, c);
+  if (threadIdx.x < 64) {
+    if (cut.parts == 1) teach<true>(a, own, teacher, c);
+    else name(own, teacher);
+  }
   marks.clear();
   marks.put_singles(row, own);
   Running run = running(c);
   add_tail<T, NT, U, kStream>(run, a, row, own, in, c, marks, r);
+  without_masked<T, NT, false>(run, row, in, c, [&](int64_t column) { return is_named(teacher, column, a.k); });
   if (a.k > 0) __syncthreads();  // a part without tiles has had none since put_singles
   if (single.column >= 0 && !marks.single()) add_one<false>(run, single.logit(), c);
   const Sum t = block_join(finished(run), lds);
@@ -1567,6 +1614,8 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
     load_tile<T, NT, more, kKeep>(row, rest.lo, q);
     add_tail<T, NT, more, kKeep>(run, a, row, own, rest, c, more_marks, q);
   }
+  without_masked<T, NT, false>(run, row, Range{first, in.hi}, c,
+                               [&](int64_t column) { return is_named(teacher, column, a.k); });
   if (single.column >= 0 && !marks.single()) add_one<false>(run, single.logit(), c);
   const Sum t = block_join(finished(run), lds);
   const Taught m = teacher.m;

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests._helpers import announce, host, require_gpu
-from tests.test_gpu_logits import check_distill, check_logprobs, dev, make, put, teacher_of
+from tests.test_gpu_logits import check_distill, check_logprobs, dev, make, near, put, teacher_of
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -59,3 +59,51 @@ def test_logits_just_above_the_mask_bound(vocab):
         ids[:, j] = (vocab // 2 + j) % vocab
     for tail in (True, False):
         check_distill(torch, z, "f32", ids, a, tokens, tail, 1.0, None, None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [7, 300, 20000, 140001])
+def test_masked_logits_close_to_the_unmasked(vocab, dtype):
+    """Columns at or just below the bound count nothing, also beside unmasked
+    ones a few units away. n equal unmasked logits: H = -ln p = ln n. bf16: the
+    scale puts neighbouring values on both sides."""
+    torch = require_gpu()
+    import bit_block_scaled_bf16_amd as nv
+
+    announce(f"masked logits close by {vocab} {dtype}")
+    if dtype == "f32":
+        scale, live_z, masked_z = 1.0, ABOVE, [-1e8, -100000008.0, -100000080.0]
+    else:
+        # -1e8 / scale lies between two neighbours of bf16, right below the upper
+        live_z, masked_z = np.float32(-99614720.0), [-100139008.0, -100663296.0]
+        scale = float(np.float32(1e8 * (1.0 - 2.0 ** -22) / 99614720.0))
+    masked_z = np.array(masked_z, np.float32)
+    scaled = lambda v: v.astype(np.float64) * np.float64(np.float32(scale))  # noqa: E731
+    assert scaled(live_z) > -1e8 and (scaled(masked_z) <= -1e8).all()
+    rng = np.random.default_rng(vocab)
+    z = rng.choice(masked_z, (4, vocab))
+    z[0, vocab // 2] = live_z
+    z[1, ::3] = live_z
+    z[2, : vocab // 2] = live_z
+    z[3, vocab - 1] = z[3, 0] = live_z
+    n = (z == live_z).sum(1)
+    tokens = np.array([0, 1, vocab - 1, 1], np.int64)  # masked ones
+    r = nv.token_logprobs(put(torch, z, dtype, 3, 1), dev(torch, tokens), top_k=2, scale=scale)
+    tol = 2 * equal_tolerance(vocab) + U * np.log(n)
+    assert np.isneginf(host(r.logp)).all()
+    assert (np.abs(host(r.entropy) - np.log(n)) <= tol * (10 + np.log(n))).all(), host(r.entropy)
+    assert (np.abs(host(r.top_logp)[:, 0] + np.log(n)) <= tol).all()
+    assert (host(r.top_ids)[0] == [vocab // 2, -1]).all()
+    ids = np.full((4, 1), -1, np.int32)
+    ids[1:, 0] = [0, 0, 0]
+    a = np.zeros((4, 1), np.float32)
+    d = nv.distill(put(torch, z, dtype, 3, 1), dev(torch, ids), dev(torch, a), dev(torch, (z == live_z).argmax(1)), scale=scale)
+    assert (np.abs(host(d.logp) + np.log(n)) <= tol).all()
+    assert (np.abs(host(d.loss)[1:] - np.log(n)[1:]) <= 4 * tol[1:]).all()
+    if vocab >= 300:  # alternatives at every place of a vector, in a row of enough unmasked logits
+        ids = np.tile(np.arange(8, dtype=np.int32), (4, 1))
+        d8 = nv.distill(put(torch, z, dtype, 3, 1), dev(torch, ids), dev(torch, np.full((4, 8), -np.log(8), np.float32)), tail=False,
+                        scale=scale)
+        assert abs(host(d8.loss)[2] - np.log(n[2] / 8)) <= 4 * tol[2] + 8 * U * np.log(8)
+    lse = scaled(z).max(1) + np.log(n)
+    near(host(d.lse), lse, 4 * U * 1e8, "lse")

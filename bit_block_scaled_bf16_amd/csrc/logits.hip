@@ -1624,9 +1624,11 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
     flat_pass<T, NT>(row, dz, in, false, c);
     return;
   }
-  // as in the backward kernel, with the sums themselves
-  const float share = exp2_hw(shift_of(t.r, s.whole.r)) / s.whole.s;
-  Factor f = {(g.gk * (m.masses + m.rest) - g.gl) * share, 0.0f, t.r};
+  // as in the backward kernel, with the sums themselves; without a tail against
+  // the whole, above which no logit lies far (a masked one does above kNoRef)
+  const float ref = t.s != 0.0f ? t.r : s.whole.r;
+  const float share = exp2_hw(shift_of(ref, s.whole.r)) / s.whole.s;
+  Factor f = {(g.gk * (m.masses + m.rest) - g.gl) * share, 0.0f, ref};
   if (m.rest != 0.0f && g.gk != 0.0f && t.s != 0.0f) f.a -= g.gk * m.rest / t.s;
   f.a *= a.scale;
   if (is_nan_row(a, m, g, f)) {

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from tests._helpers import announce, host, require_gpu
-from tests.test_gpu_logits import check_distill, check_logprobs, dev, make, near, put, teacher_of
+from tests.test_gpu_logits import bf16, check_distill, check_logprobs, dev, make, near, put, teacher_of
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -107,3 +107,34 @@ def test_masked_logits_close_to_the_unmasked(vocab, dtype):
         assert abs(host(d8.loss)[2] - np.log(n[2] / 8)) <= 4 * tol[2] + 8 * U * np.log(8)
     lse = scaled(z).max(1) + np.log(n)
     near(host(d.lse), lse, 4 * U * 1e8, "lse")
+
+
+# ---------------------------------------------------------------------------
+# Nothing unmasked outside the alternatives
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.125])
+@pytest.mark.parametrize("mask", [-1e8, -1.2e8, -1.38e8, -1.5e8, -1e9])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [40, 3000, 40001, 140001])
+def test_step_with_masks_of_finite_values_outside_the_alternatives(vocab, dtype, mask, scale):
+    """A grammar that leaves fewer choices than the teacher names, masked by a
+    number as a user writes it: no gradient outside, in the step as in the
+    backward call."""
+    torch = require_gpu()
+    announce(f"no tail {vocab} {dtype} mask {mask} scale {scale}")
+    mask = mask / scale
+    rows, k = 3, 6
+    z = make(rows, vocab, dtype, 4)
+    ids, a = teacher_of(z, k, 3, ragged=False)
+    out = np.ones(z.shape, bool)
+    np.put_along_axis(out, ids, False, 1)
+    z[out] = mask
+    z[1, ids[1, 2:]] = mask                        # some of the alternatives too
+    z = bf16(z) if dtype == "bf16" else z
+    a[2] -= np.log(np.exp(a[2].astype(np.float64)).sum()).astype(np.float32)
+    labels = np.array([ids[0, 0], ids[1, 1], (ids[2, 0] + 1) % vocab], np.int64)
+    g = np.array([0.5, 1.0, 1.5], np.float32)
+    for tail in (True, False):
+        check_distill(torch, z, dtype, ids, a, labels, tail, scale, g, -g)

@@ -907,11 +907,40 @@ __device__ __forceinline__ T from_word(uint32_t w) {
   else return __uint_as_float(w);
 }
 
+// Whether masked logits may lie so near to ref that their p is not 0 by itself:
+// they get it below 2^-9000 only where ref is above kFirstRef (in log2; in nats
+// -9.9992e7, taken a little higher).
+template <int kFrom>
+__device__ __forceinline__ bool beside_masked(const Factor& f) {
+  return f.ref < (kFrom == kFromRef ? kFirstRef : -0.9999e8f);
+}
+
+// The gradient of rows beside masked logits: a vector at a time, masked ones by
+// themselves.
+template <typename T, int NT, bool kEntropy, int kFrom>
+__device__ __forceinline__ void beside_masked_pass(const Row<T>& row, T* dz, const Range& in, float scale,
+                                                   const Factor& f, const Scale& c) {
+  constexpr int n = Vec<T>::n;
+#pragma unroll 1
+  for (int v = in.lo + static_cast<int>(threadIdx.x); v < in.hi; v += NT) {
+    if (!row.whole(v)) continue;
+    float x[n];
+    Vec<T>::unpack(load_vec<T, kStream>(row.z + row.column(v)), x);
+#pragma unroll
+    for (int e = 0; e < n; ++e) x[e] = x[e] <= c.low ? -kInf : x[e];
+    store_whole(dz, row, v, gradient_of<T, kEntropy, kFrom>(Vec<T>::pack(x), scale, f, c));
+  }
+}
+
 // The gradient of the tiles of `in`, the first of which has been requested into
 // r.
 template <typename T, int NT, int U, bool kEntropy, int kFrom>
 __device__ __forceinline__ void gradient_pass(const Row<T>& row, T* dz, const Range& in, float scale,
                                               const Factor& f, const Scale& c, Raw (&r)[U]) {
+  if (beside_masked<kFrom>(f)) {
+    beside_masked_pass<T, NT, kEntropy, kFrom>(row, dz, in, scale, f, c);
+    return;
+  }
   for (int first = in.lo; first < in.hi;) {
 #pragma unroll
     for (int u = 0; u < U; ++u) r[u] = gradient_of<T, kEntropy, kFrom>(r[u], scale, f, c);
@@ -940,8 +969,9 @@ struct Single {
   __device__ __forceinline__ float logit() const { return column >= 0 ? load_one(&z) : -kInf; }
   template <bool kEntropy, int kFrom>
   __device__ __forceinline__ void gradient(T* dz, float scale, const Factor& f, const Scale& c) const {
-    if (column >= 0)
-      dz[column] = from_word<T>(gradient_of<T, kEntropy, kFrom>(Raw{as_word(z), 0u, 0u, 0u}, scale, f, c)[0]);
+    if (column < 0) return;
+    const Raw own = gradient_of<T, kEntropy, kFrom>(Raw{as_word(z), 0u, 0u, 0u}, scale, f, c);
+    dz[column] = logit() <= c.low ? T{} : from_word<T>(own[0]);
   }
 };
 
@@ -1640,15 +1670,19 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
       a, row, in, own, teacher, g, x_label, c,
       [&](float x) { return exp2_hw(fma_(x, c.c, -s.whole.r)) / s.whole.s; },
       [&](float x) { return exp2_hw(fma_(x, c.c, -f.ref)) * f.a; });
+  if (beside_masked<kFromRef>(f)) {
+    beside_masked_pass<T, NT, false, kFromRef>(row, dz, Range{first, in.hi}, a.scale, f, c);
+  } else {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int v = first + u * NT + static_cast<int>(threadIdx.x);
-    if (row.whole(v)) store_whole(dz, row, v, gradient_of<T, false, kFromRef>(r[u], a.scale, f, c));
-  }
-  if constexpr (kMore) {
-    Raw q[more];
-    load_tile<T, NT, more, kStream>(row, rest.lo, q);
-    gradient_pass<T, NT, more, false, kFromRef>(row, dz, rest, a.scale, f, c, q);
+    for (int u = 0; u < U; ++u) {
+      const int v = first + u * NT + static_cast<int>(threadIdx.x);
+      if (row.whole(v)) store_whole(dz, row, v, gradient_of<T, false, kFromRef>(r[u], a.scale, f, c));
+    }
+    if constexpr (kMore) {
+      Raw q[more];
+      load_tile<T, NT, more, kStream>(row, rest.lo, q);
+      gradient_pass<T, NT, more, false, kFromRef>(row, dz, rest, a.scale, f, c, q);
+    }
   }
   single.template gradient<false, kFromRef>(dz, a.scale, f, c);
   __syncthreads();

@@ -4,10 +4,13 @@ against values worked by hand."""
 import numpy as np
 import pytest
 
+import oracle as o
 from tests._helpers import announce, host, require_gpu
-from tests.test_gpu_logits import bf16, check_distill, check_logprobs, dev, make, near, put, teacher_of
+from tests.test_gpu_logits import (bf16, check_distill, check_gradient, check_logprobs, dev, make, near, put,
+                                   teacher_of)
 
 pytestmark = pytest.mark.gpu
+L = o.logits
 U = 2.0 ** -24
 
 
@@ -107,6 +110,54 @@ def test_masked_logits_close_to_the_unmasked(vocab, dtype):
         assert abs(host(d8.loss)[2] - np.log(n[2] / 8)) <= 4 * tol[2] + 8 * U * np.log(8)
     lse = scaled(z).max(1) + np.log(n)
     near(host(d.lse), lse, 4 * U * 1e8, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [7, 300, 20000, 140001])
+def test_gradient_of_masked_logits_close_to_the_unmasked(vocab, dtype):
+    """It is 0, whatever the neighbours."""
+    torch = require_gpu()
+    import bit_block_scaled_bf16_amd as nv
+
+    announce(f"gradient of masked logits close by {vocab} {dtype}")
+    if dtype == "f32":
+        scale, live_z, masked_z = 1.0, ABOVE, [-1e8, -100000008.0, -100000080.0]
+    else:
+        live_z, masked_z = np.float32(-99614720.0), [-100139008.0, -100663296.0]
+        scale = float(np.float32(1e8 * (1.0 - 2.0 ** -22) / 99614720.0))
+    rng = np.random.default_rng(vocab)
+    z = rng.choice(np.array(masked_z, np.float32), (5, vocab))
+    z[0, vocab // 2] = live_z
+    z[1, ::3] = live_z
+    z[2, : vocab // 2] = live_z
+    z[3, vocab - 1] = z[3, 0] = live_z
+    z[4, ::2] = live_z
+    live = z == live_z
+    # an lse right on the unmasked logits (float32 steps there are 8 wide), as the forward call may round it
+    lse = np.full(5, np.float32(-99999992.0), np.float32) if dtype == "f32" else np.float32(live_z * np.float32(scale)) * np.ones(5, np.float32)
+    one = torch.ones(5, device="cuda")
+    zt = put(torch, z, dtype, 3, 1)
+    tokens = dev(torch, live.argmax(1))
+    off = lambda t: host(t.float())[~live]  # noqa: E731
+    on = lambda t: host(t.float())[live]  # noqa: E731
+    d = nv.token_logprobs_backward(zt, tokens, dev(torch, lse), one, one, one, scale)
+    ones, label = np.ones(5, np.float32), live.argmax(1)
+    check_gradient(host(d.float()), L.token_logprobs_backward(z, label, lse, ones, ones, ones, scale), z, scale, lse,
+                   3 * ones, dtype)
+    assert (off(d) == 0).all() and (on(d) != 0).any()
+    ids = label.astype(np.int32)[:, None]
+    a = np.full((5, 1), -0.5, np.float32)
+    t = (dev(torch, ids), dev(torch, a), tokens)
+    for tail in (True, False):
+        d = nv.distill_backward(zt, *t, dev(torch, lse), dev(torch, lse), one, one, tail, scale)
+        ref = L.distill_backward(z, ids, a, label, lse, lse, ones, ones, tail, scale)
+        check_gradient(host(d.float()), ref, z, scale, lse, 3 * ones, dtype, 2 * live)
+        assert (off(d) == 0).all(), tail
+        d = nv.distill_step(zt, *t, d_loss=one, d_logp=one, tail=tail, scale=scale)[1]
+        assert (off(d) == 0).all() and np.isfinite(on(d)).all(), tail
+        same = zt.clone()
+        nv.distill_step(same, *t, d_loss=one, d_logp=one, tail=tail, scale=scale, out=same)
+        assert (off(same) == 0).all() and np.isfinite(on(same)).all(), tail
 
 
 # ---------------------------------------------------------------------------

@@ -1478,6 +1478,9 @@ __global__ __launch_bounds__(NT) void distill_join_kernel(LogitsLaunch a, Cut cu
 struct Upstream {
   float gk, gl;
   int64_t label;
+
+  // gk v; 0 where the teacher has no weight, whatever it holds
+  __device__ __forceinline__ float of_teacher(float v) const { return gk != 0.0f ? gk * v : 0.0f; }
 };
 
 __device__ __forceinline__ Upstream upstream(const LogitsLaunch& a, int64_t at) {
@@ -1530,7 +1533,7 @@ __device__ __forceinline__ Special special_columns(const LogitsLaunch& a, const 
     if (here && !(own.x[h] <= c.low)) {
       const float p = prob(own.x[h]);
       const float q = doubled ? mass_of(t, id, a.k) : t.q[(threadIdx.x & 63) + 64 * h];
-      v = (g.gk * (all * p - q) + g.gl * ((id == g.label ? 1.0f : 0.0f) - p)) * a.scale;
+      v = (g.of_teacher(all * p - q) + g.gl * ((id == g.label ? 1.0f : 0.0f) - p)) * a.scale;
     }
     s.column[h] = here ? id : -1;
     s.value[h] = v;
@@ -1574,7 +1577,7 @@ __global__ __launch_bounds__(NT) void distill_backward_kernel(LogitsLaunch a, Cu
   // = e^(s - L_r) ((gk all - gl) e^(L_r - L) - gk rest): one exponential, and
   // no factor above 1, however little of the student's mass lies there.
   const bool from_tail = m.rest != 0.0f && g.gk != 0.0f && lse_tail != -kInf;
-  const float ref = from_tail ? lse_tail : lse, both = g.gk * (m.masses + m.rest) - g.gl;
+  const float ref = from_tail ? lse_tail : lse, both = g.of_teacher(m.masses + m.rest) - g.gl;
   const float factor = (from_tail ? both * expf(lse_tail - lse) - g.gk * m.rest : both) * a.scale;
   const Factor f = {factor, 0.0f, ref};
   if (is_nan_row(a, m, g, f)) {
@@ -1658,7 +1661,7 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
   // the whole, above which no logit lies far (a masked one does above kNoRef)
   const float ref = t.s != 0.0f ? t.r : s.whole.r;
   const float share = exp2_hw(shift_of(ref, s.whole.r)) / s.whole.s;
-  Factor f = {(g.gk * (m.masses + m.rest) - g.gl) * share, 0.0f, ref};
+  Factor f = {(g.of_teacher(m.masses + m.rest) - g.gl) * share, 0.0f, ref};
   if (m.rest != 0.0f && g.gk != 0.0f && t.s != 0.0f) f.a -= g.gk * m.rest / t.s;
   f.a *= a.scale;
   if (is_nan_row(a, m, g, f)) {

@@ -7,7 +7,7 @@ import pytest
 import oracle as o
 from tests._helpers import announce, host, require_gpu
 from tests.test_gpu_logits import (bf16, check_distill, check_gradient, check_logprobs, dev, make, near, put,
-                                   teacher_of)
+                                   teacher_of, tol_lse)
 
 pytestmark = pytest.mark.gpu
 L = o.logits
@@ -189,3 +189,39 @@ def test_step_with_masks_of_finite_values_outside_the_alternatives(vocab, dtype,
     g = np.array([0.5, 1.0, 1.5], np.float32)
     for tail in (True, False):
         check_distill(torch, z, dtype, ids, a, labels, tail, scale, g, -g)
+
+
+# ---------------------------------------------------------------------------
+# Rows that take no gradient from their teacher
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("vocab", [50, 20000])
+def test_a_teacher_without_weight_is_not_looked_at(vocab, tail):
+    """d_loss 0 beside a label's gradient: what the teacher holds is no matter."""
+    torch = require_gpu()
+    import bit_block_scaled_bf16_amd as nv
+
+    announce(f"a teacher without weight {vocab} tail={tail}")
+    rows = 3
+    z = make(rows, vocab, "f32", 6)
+    ids, a = teacher_of(z, 5, 3, ragged=False)
+    a[0, 2], a[1, 3] = np.nan, np.inf
+    labels = np.array([1, ids[1, 3], ids[2, 0]], np.int64)
+    gl, zero = np.array([1.0, -2.0, 0.5], np.float32), np.zeros(rows, np.float32)
+    f = L.distill(z, None, None, labels)
+    lse = f["lse"].astype(np.float32)
+    ref = L.distill_backward(z, None, None, labels, lse, lse, None, gl)
+    zt = put(torch, z, "f32")
+    t = (dev(torch, ids), dev(torch, a), dev(torch, labels))
+    one = np.zeros(z.shape)
+    one[np.arange(rows), labels] = np.abs(gl)
+    for weight in (None, dev(torch, zero)):
+        d = nv.distill_backward(zt, *t, dev(torch, lse), dev(torch, lse), weight, dev(torch, gl), tail)
+        check_gradient(host(d), ref, z, 1.0, lse, np.abs(gl), "f32", one)
+        d = nv.distill_step(zt, *t, d_loss=weight, d_logp=dev(torch, gl), tail=tail)[1]
+        # its own L: off by at most the forward's tolerance, and u |L| from its rounding to float32
+        p = np.exp(z.astype(np.float64) - f["lse"][:, None])
+        slack = p * np.abs(gl)[:, None] * (2 * tol_lse(z, 1.0, f["lse"]) + 2 * U * np.abs(f["lse"]))[:, None] * 2 / (8 * U)
+        check_gradient(host(d), ref, z, 1.0, lse, np.abs(gl), "f32", one + slack)

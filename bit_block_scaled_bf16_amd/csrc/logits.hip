@@ -1226,10 +1226,7 @@ __device__ __forceinline__ void teach(const LogitsLaunch& a, const Alternatives&
     }
   } else {
 #pragma unroll
-    for (int h = 0; h < kOwn; ++h) {
-      t.id[lane + 64 * h] = -1;
-      t.q[lane + 64 * h] = 0.0f;
-    }
+    for (int h = 0; h < kOwn; ++h) t.id[lane + 64 * h] = -1;
   }
   if (lane == 0) {
     t.m.rest = rest;
@@ -1404,7 +1401,7 @@ __device__ __forceinline__ RowSums finish_distill(const LogitsLaunch& a, int64_t
                                                   const Scale& c) {
   const RowSums s = {tail, a.k > 0 ? join(tail, t.m.members) : tail};
   float loss = 0.0f;
-  if (threadIdx.x < 64) loss = divergence(own, s.whole, tail, t, c);
+  if (a.k > 0 && threadIdx.x < 64) loss = divergence(own, s.whole, tail, t, c);
   if (threadIdx.x == 0) {
     const float l2 = log2_hw(s.whole.s), tail_l2 = log2_hw(tail.s);
     bool bad = s.whole.s != s.whole.s || t.m.bad;

@@ -471,7 +471,7 @@ enum { NVFP4_DISTILL_RENORM = 0, NVFP4_DISTILL_TAIL = 1 };
  *              row names twice counts with both masses and is one column.
  *   loss       out [rows]: sum_j q_j (ln q_j - s_{id_j} + L)
  *              + q_r (ln q_r - L_r + L); terms of mass 0 are 0. +inf where the
- *              teacher has mass on masked columns alone.
+ *              teacher has mass on masked columns alone; 0 when k == 0.
  *   labels, logp  as tokens, logp of nvfp4_token_logprobs (NULL both, or not).
  *   lse, lse_tail  out [rows]: L and L_r.
  */

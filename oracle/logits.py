@@ -14,7 +14,7 @@ are the textbook definitions. With s_v = scale * z_v over the unmasked columns
 * teacher masses from log probabilities a_j of the present ids: q_j = e^(a_j)
   with the rest q_r = 1 - sum q (0 below 1e-6), or q = softmax(a), q_r = 0.
 * divergence: sum q_j (ln q_j - ln p_id_j) + q_r (ln q_r - ln p_r), p_r the
-  student's mass on the columns that are no alternative.
+  student's mass on the columns that are no alternative. 0 without a teacher.
 
 A row that holds NaN or an s_v > 1e8 (+inf), or an index beyond the vocabulary, gives
 NaN in what depends on it.
@@ -141,8 +141,7 @@ def distill(z, ids=None, logp=None, labels=None, tail: bool = True, scale: float
         out["lse"][i], out["lse_tail"][i] = lse, lse_tail
         if labels is not None:
             out["logp"][i] = _logp(s, lse, int(labels[i]))
-        q, rest = (teacher(row_ids, logp[i], tail) if ids is not None
-                   else (np.zeros(0), 1.0 if tail else 0.0))
+        q, rest = teacher(row_ids, logp[i], tail) if ids is not None else (np.zeros(0), 0.0)
         if np.isnan(lse) or any(j >= vocab for j in row_ids):
             out["loss"][i] = np.nan
             continue

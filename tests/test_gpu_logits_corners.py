@@ -6,7 +6,7 @@ import pytest
 
 import oracle as o
 from tests._helpers import announce, host, require_gpu
-from tests.test_gpu_logits import (bf16, check_distill, check_gradient, check_logprobs, dev, make, near, put,
+from tests.test_gpu_logits import (LOW, bf16, check_distill, check_gradient, check_logprobs, dev, make, near, put,
                                    teacher_of, tol_lse)
 
 pytestmark = pytest.mark.gpu
@@ -225,3 +225,36 @@ def test_a_teacher_without_weight_is_not_looked_at(vocab, tail):
         p = np.exp(z.astype(np.float64) - f["lse"][:, None])
         slack = p * np.abs(gl)[:, None] * (2 * tol_lse(z, 1.0, f["lse"]) + 2 * U * np.abs(f["lse"]))[:, None] * 2 / (8 * U)
         check_gradient(host(d), ref, z, 1.0, lse, np.abs(gl), "f32", one + slack)
+
+
+# ---------------------------------------------------------------------------
+# No teacher
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("vocab", [9, 3000, 40001])
+def test_without_a_teacher_there_is_no_divergence(vocab, tail):
+    """Also in a row with nothing unmasked (a padded position of a cross entropy
+    step): its loss is 0 and not in the way of a mean."""
+    torch = require_gpu()
+    import bit_block_scaled_bf16_amd as nv
+
+    announce(f"no teacher {vocab} tail={tail}")
+    z = make(4, vocab, "f32", 8)
+    z[1], z[2] = -np.inf, LOW["f32"]
+    labels = np.array([1, -1, 2, 0], np.int64)
+    want = L.distill(z, None, None, labels, tail)
+    assert (want["loss"] == 0).all()
+    zt = put(torch, z, "f32")
+    w = torch.ones(4, device="cuda")
+    r = nv.distill(zt, None, None, dev(torch, labels), tail=tail)
+    s, d = nv.distill_step(zt, None, None, dev(torch, labels), d_loss=w, d_logp=-w, tail=tail)
+    for x in (r, s):
+        assert (host(x.loss) == 0).all(), host(x.loss)
+        assert np.isneginf(host(x.lse)[1:3]).all() and host(x.logp)[1] == 0 and np.isneginf(host(x.logp)[2])
+    assert (host(d)[1:3] == 0).all()
+    z[3, 4] = np.nan  # still told
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = nv.distill(put(torch, z, "f32"), None, None, dev(torch, labels), tail=tail, dev_status=flag)
+    assert np.isnan(host(r.loss)[3]) and (host(r.loss)[:3] == 0).all() and int(flag.item()) == 1

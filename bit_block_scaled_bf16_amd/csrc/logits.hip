@@ -1068,11 +1068,15 @@ constexpr int kOwn = NVFP4_LOGITS_MAX_K / 64;
 struct Alternatives {
   int id[kOwn];    // as given; -1 in the other waves
   float a[kOwn];   // log probability
-  float x[kOwn];   // the student's logit; -inf where there is none
+  float x[kOwn];   // the student's logit; -inf where there is none, or it is not wanted
 };
 
-template <typename T>
-__device__ __forceinline__ Alternatives load_alternatives(const LogitsLaunch& a, const T* z, int64_t at) {
+// wanted(id): whether the caller uses the logit of id. A part of a row reads no
+// others': the gradient of 64 rows of 32768 float32 logits (8.4 MB) with 128
+// alternatives reads 9.1 MB so, and 16.0 with all of them; and in place the other
+// parts overwrite theirs meanwhile.
+template <typename T, typename F>
+__device__ __forceinline__ Alternatives load_alternatives(const LogitsLaunch& a, const T* z, int64_t at, F wanted) {
   Alternatives m;
 #pragma unroll
   for (int h = 0; h < kOwn; ++h) {
@@ -1087,7 +1091,7 @@ __device__ __forceinline__ Alternatives load_alternatives(const LogitsLaunch& a,
   }
 #pragma unroll
   for (int h = 0; h < kOwn; ++h)
-    if (m.id[h] >= 0 && m.id[h] < a.vocab) m.x[h] = load_one(z + m.id[h]);
+    if (m.id[h] >= 0 && m.id[h] < a.vocab && wanted(m.id[h])) m.x[h] = load_one(z + m.id[h]);
   return m;
 }
 
@@ -1429,7 +1433,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(LogitsLaunch a, Cut cut) {
   const Row<T> row = row_at(z, a.vocab, z);
   const Range in = range_of<NT, U>(cut, static_cast<int>(blockIdx.x % cut.parts), row.vectors());
   const Scale c = scale_of(a.scale);
-  const Alternatives own = load_alternatives(a, z, at);
+  const Alternatives own = load_alternatives(a, z, at, [&](int) { return cut.parts == 1; });
   float x_token;
   const int64_t token = load_token(a, z, at, &x_token);
   Single<T> single;
@@ -1463,7 +1467,7 @@ __global__ __launch_bounds__(NT) void distill_join_kernel(LogitsLaunch a, Cut cu
   const int64_t at = blockIdx.x;
   const T* z = static_cast<const T*>(a.z) + at * a.ldz;
   const Scale c = scale_of(a.scale);
-  const Alternatives own = load_alternatives(a, z, at);
+  const Alternatives own = load_alternatives(a, z, at, [](int) { return true; });
   float x_token;
   const int64_t token = load_token(a, z, at, &x_token);
   if (threadIdx.x < 64) teach<true>(a, own, teacher, c);
@@ -1560,9 +1564,9 @@ __global__ __launch_bounds__(NT) void distill_backward_kernel(LogitsLaunch a, Cu
     flat_pass<T, NT>(row, dz, in, false, c);
     return;
   }
-  const Alternatives own = load_alternatives(a, z, at);
+  const Alternatives own = load_alternatives(a, z, at, [&](int id) { return holds(row, in, id); });
   float x_label = 0.0f;
-  if (threadIdx.x == 0 && g.label >= 0 && g.label < a.vocab) x_label = load_one(z + g.label);
+  if (threadIdx.x == 0 && holds(row, in, g.label)) x_label = load_one(z + g.label);
   Single<T> single;
   single.load(row, in);
   Raw r[U];
@@ -1616,7 +1620,7 @@ __global__ __launch_bounds__(NT) void distill_step_kernel(LogitsLaunch a) {
   // whole vectors from the first whole one
   const int first = kMore || in.hi <= NT * U ? 0 : (row.skip + n - 1) / n;
   const Scale c = scale_of(a.scale);
-  const Alternatives own = load_alternatives(a, z, at);
+  const Alternatives own = load_alternatives(a, z, at, [](int) { return true; });
   float x_token;
   const int64_t token = load_token(a, z, at, &x_token);
   const Upstream g = upstream(a, at);

@@ -48,9 +48,14 @@ class Distilled(NamedTuple):
     lse_tail: "object"  # the same over the columns that are no alternative
 
 
-def _rows(n, rows, device):
-    """n float32 vectors of a value per row, and their pointers, in one
-    allocation (half the time of n)."""
+def _rows(n, rows, device, apart=False):
+    """n float32 vectors of a value per row, and their pointers: in one
+    allocation (half the time of n), or each a tensor of its own, as an autograd
+    function's outputs have to be (a view among several of one block may not be
+    changed in place, and shares its version with them)."""
+    if apart:
+        out = [torch.empty(rows, dtype=torch.float32, device=device) for _ in range(n)]
+        return out, [t.data_ptr() for t in out]
     block = torch.empty(n, rows, dtype=torch.float32, device=device)
     at = block.data_ptr()
     return block.unbind(0), [at + 4 * rows * i for i in range(n)]
@@ -74,10 +79,14 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, scale: float = 1.0, entr
                    dev_status=None) -> TokenLogprobs:
     """Log probabilities of the tokens (int64 [rows], or None), the entropy and
     the top_k most probable tokens of each row (ties to the lowest id)."""
+    return _token_logprobs(logits, tokens, top_k, scale, entropy, dev_status)
+
+
+def _token_logprobs(logits, tokens, top_k, scale, entropy, dev_status, apart=False):
     matrix, stream = _lib._logits(logits)
     rows, device = matrix[2], logits.device
     given = _lib._vector(tokens, "tokens", torch.int64, (rows,), logits)
-    out, at = _rows(1 + (given is not None) + bool(entropy), rows, device)
+    out, at = _rows(1 + (given is not None) + bool(entropy), rows, device, apart)
     logp = h = p_logp = p_h = ids = top = p_ids = p_top = None
     if given is not None:
         logp, p_logp = out[1], at[1]
@@ -112,9 +121,13 @@ def distill(logits, teacher_ids, teacher_logp, labels=None, tail: bool = True, s
     probabilities (int64 [rows], or None). tail: the teacher's remaining mass
     is compared with the student's outside the alternatives; else the
     alternatives are renormalised to 1."""
+    return _distill(logits, teacher_ids, teacher_logp, labels, tail, scale, dev_status)
+
+
+def _distill(logits, teacher_ids, teacher_logp, labels, tail, scale, dev_status, apart=False):
     matrix, stream = _lib._logits(logits)
     teacher = _lib._teacher(logits, teacher_ids, teacher_logp, labels)
-    out, at = _rows(3 + (labels is not None), matrix[2], logits.device)
+    out, at = _rows(3 + (labels is not None), matrix[2], logits.device, apart)
     ws, p_ws, n_ws = _workspace(matrix, teacher[2], logits.device)
     _lib._check("nvfp4_distill", _lib.lib().nvfp4_distill(
         *matrix, *teacher, _mode(tail), scale, at[0], None if labels is None else at[3], at[1],
@@ -163,7 +176,7 @@ class TokenLogprobsFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, tokens, scale: float):
-        r = token_logprobs(logits, tokens, scale=scale)
+        r = _token_logprobs(logits, tokens, 0, scale, True, None, apart=True)
         ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
         ctx.scale = scale
         ctx.set_materialize_grads(False)
@@ -185,7 +198,7 @@ class DistillFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, teacher_ids, teacher_logp, labels, tail: bool, scale: float):
-        r = distill(logits, teacher_ids, teacher_logp, labels, tail, scale)
+        r = _distill(logits, teacher_ids, teacher_logp, labels, tail, scale, None, apart=True)
         ctx.save_for_backward(logits, teacher_ids, teacher_logp, labels, r.lse, r.lse_tail)
         ctx.how = (tail, scale)
         ctx.set_materialize_grads(False)

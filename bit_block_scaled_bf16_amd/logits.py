@@ -25,6 +25,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -167,7 +168,7 @@ def distill_step(logits, teacher_ids, teacher_logp, labels=None, d_loss=None, d_
 
 
 # ---------------------------------------------------------------------------
-# Differentiable forms
+# Differentiable forms (once: a second derivative raises)
 # ---------------------------------------------------------------------------
 
 
@@ -183,6 +184,7 @@ class TokenLogprobsFunction(torch.autograd.Function):
         return r.logp, r.entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_logp, d_entropy):
         logits, tokens, lse, entropy = ctx.saved_tensors
         if d_logp is None and d_entropy is None:
@@ -205,6 +207,7 @@ class DistillFunction(torch.autograd.Function):
         return r.loss, r.logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_loss, d_logp):
         if d_loss is None and d_logp is None:
             return (None,) * 6

@@ -58,3 +58,15 @@ def test_outputs_share_no_storage():
         y = form(z.clone().requires_grad_(True))
         assert y[0].untyped_storage().data_ptr() != y[1].untyped_storage().data_ptr(), name
         assert not y[0]._is_view() and not y[1]._is_view(), name
+
+
+@pytest.mark.parametrize("name", ["token_logprobs", "distill"])
+def test_second_derivatives_are_refused(name):
+    """They are not computed: asking for one raises instead of dropping it."""
+    torch = require_gpu()
+    announce(f"second derivative {name}")
+    z, forms = both(torch)
+    x = z.clone().requires_grad_(True)
+    g, = torch.autograd.grad(sum(t.sum() for t in forms[name](x)), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.square().sum().backward()

@@ -25,9 +25,9 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _lib
+from .autograd import once_differentiable
 
 
 class TokenLogprobs(NamedTuple):

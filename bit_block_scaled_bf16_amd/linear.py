@@ -29,6 +29,7 @@ import torch
 
 from . import (BLOCK_2D, OUT_COL, OUT_ROW, ROUND_RN, ROUND_SR, gemm, quantize, quantize_row_rht,
                rht_quantize)
+from .autograd import once_differentiable
 
 
 class NVFP4LinearFunction(torch.autograd.Function):
@@ -50,6 +51,7 @@ class NVFP4LinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rht_seed, sr_seed, sr_offset = ctx.seeds
         dy = dy.contiguous()

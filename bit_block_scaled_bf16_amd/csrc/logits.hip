@@ -1884,11 +1884,17 @@ int launch_distill_backward(const LogitsLaunch& a, hipStream_t stream) {
 
 int launch_distill_step(const LogitsLaunch& a, hipStream_t stream) {
   const int64_t whole = a.vocab / (a.z_bf16 ? 8 : 4);  // vectors
-  const Plan p = plan_forward(a);
-  // A workgroup takes a row where that fills the GPU. One of 1024 threads has a
-  // CU to itself, and for few rows the split kernels are quicker: a row of
-  // 131072 bf16 logits takes 28 us against 25 for 64 rows, 31 against 34 for 128.
-  if (whole <= 8192 || a.rows >= 128 || p.cut.parts == 1)
+  // A workgroup a row, or the forward and the gradient one after the other, which
+  // cut rows for few of them. Both sides, us a call with 64 alternatives:
+  //            rows:   1            32           64           96
+  //   131072 bf16    18.7 / 20.8  20.5 / 23.2  20.7 / 26.4  21.4 / 30.5
+  //   131072 f32     23.7 / 21.8  25.2 / 28.1  25.6 / 31.2  28.3 / 42.1
+  //   151936 bf16    23.3 / 21.2  25.7 / 25.8  26.9 / 29.8  27.5 / 33.5
+  //   230001 bf16    34.1 / 26.0  37.2 / 32.2  37.9 / 37.9  38.8 / 44.0
+  //   200001 f32     34.3 / 23.4  37.6 / 28.8  40.2 / 40.2  46.5 / 56.2
+  //   300001 bf16    40.9 / 23.1  44.7 / 25.7  46.2 / 37.6  48.2 / 45.4
+  const int64_t from = a.vocab <= 131072 ? 1 : a.vocab <= 262144 ? 64 : 128;
+  if (a.rows >= from)
     return by_rows(a, [&](const LogitsLaunch& b) {
       const auto with = [&](auto type) {
         using T = decltype(type);

@@ -1421,8 +1421,8 @@ __device__ __forceinline__ RowSums finish_distill(const LogitsLaunch& a, int64_t
 
 // The sum of the columns that are no alternative, from a bit per logit in LDS;
 // the alternatives' part comes from the first wave. Bound by HBM: 2048 x 131072
-// bf16 with 64 alternatives takes 83 us (6.4 TB/s, 97 % of a read's rate at that
-// size), the vector unit 0.62 busy.
+// bf16 with 64 alternatives takes 84 us (6.4 TB/s, 96 % of a read's rate at that
+// size), the vector unit 0.61 busy.
 template <typename T, int NT, int U>
 __global__ __launch_bounds__(NT) void distill_kernel(LogitsLaunch a, Cut cut) {
   __shared__ Teacher teacher;
@@ -1459,7 +1459,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(LogitsLaunch a, Cut cut) {
   finish_distill(a, at, token, x_token, t, own, teacher, c);
 }
 
-// Finishes rows that were cut into parts: 4 us, most of it a launch's latency.
+// Finishes rows that were cut into parts: 4.6 us, most of it a launch's latency.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void distill_join_kernel(LogitsLaunch a, Cut cut) {
   __shared__ Teacher teacher;
@@ -1547,7 +1547,7 @@ __device__ __forceinline__ Special special_columns(const LogitsLaunch& a, const 
 
 // One exponential a logit with the row's factor, the label's and the
 // alternatives' columns after the pass. Bound by HBM: 4096 x 100003 bf16 with 32
-// alternatives takes 319 us (5.1 TB/s, 94 % of a copy's rate).
+// alternatives takes 320 us (5.1 TB/s, 93 % of a copy's rate).
 template <typename T, int NT, int U>
 __global__ __launch_bounds__(NT) void distill_backward_kernel(LogitsLaunch a, Cut cut) {
   __shared__ Teacher teacher;

@@ -970,8 +970,8 @@ struct Single {
   template <bool kEntropy, int kFrom>
   __device__ __forceinline__ void gradient(T* dz, float scale, const Factor& f, const Scale& c) const {
     if (column < 0) return;
-    const Raw own = gradient_of<T, kEntropy, kFrom>(Raw{as_word(z), 0u, 0u, 0u}, scale, f, c);
-    dz[column] = logit() <= c.low ? T{} : from_word<T>(own[0]);
+    const uint32_t word = logit() <= c.low ? Vec<T>::gone : as_word(z);  // the same zeros as in a vector
+    dz[column] = from_word<T>(gradient_of<T, kEntropy, kFrom>(Raw{word, 0u, 0u, 0u}, scale, f, c)[0]);
   }
 };
 

@@ -488,7 +488,8 @@ int nvfp4_distill(const void* z, int z_dtype, int64_t rows, int64_t vocab, int64
  * with gk = d_loss and gl = d_logp of the row (0 where its label is absent),
  * and lse (L) and lse_tail (L_r) as the forward call stored them.
  *
- *   d_loss     [rows], or NULL for 0.
+ *   d_loss     [rows], or NULL for 0. A row's teacher is not looked at where it
+ *              is 0.
  *   d_logp     [rows], or NULL for 0 (then labels may be NULL). Not both NULL.
  *   lse_tail   needed in mode NVFP4_DISTILL_TAIL with d_loss; else may be NULL.
  *   dz, lddz   as in nvfp4_token_logprobs_backward.

@@ -160,6 +160,35 @@ def test_gradient_of_masked_logits_close_to_the_unmasked(vocab, dtype):
         assert (off(same) == 0).all() and np.isfinite(on(same)).all(), tail
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_do_not_depend_on_the_alignment(dtype):
+    """Their bits, the zeros' signs of masked columns among them, where columns
+    move from a vector to a single thread."""
+    torch = require_gpu()
+    import bit_block_scaled_bf16_amd as nv
+
+    announce(f"gradient bits at other alignments {dtype}")
+    z = make(4, 333, dtype, 6)
+    z[0, ::3], z[1, 1::2], z[2, 5:], z[3, :7] = -np.inf, LOW[dtype], -1e9, -2e8
+    z = bf16(z) if dtype == "bf16" else z
+    f = L.token_logprobs(z, np.zeros(4, np.int64))
+    lse, ent = dev(torch, f["lse"].astype(np.float32)), dev(torch, f["entropy"].astype(np.float32))
+    ids, a = teacher_of(z, 4, 1, ragged=False)
+    tok = dev(torch, np.array([1, 0, 2, 9], np.int64))
+    one = torch.ones(4, device="cuda")
+    bits = lambda t: t.contiguous().view(torch.int16 if dtype == "bf16" else torch.int32)  # noqa: E731
+    first = None
+    for off in range(9):
+        zt = put(torch, z, dtype, 1, off)
+        out = put(torch, z, dtype, 3, off)
+        got = [nv.token_logprobs_backward(zt, tok, lse, ent, one, -one, out=out).clone(),
+               nv.token_logprobs_backward(zt, tok, lse, None, one, None, out=out).clone(),
+               nv.distill_backward(zt, dev(torch, ids), dev(torch, a), tok, lse, lse, one, -one, out=out).clone()]
+        first = first or got
+        for x, y in zip(got, first):
+            assert torch.equal(bits(x), bits(y)), off
+
+
 # ---------------------------------------------------------------------------
 # Nothing unmasked outside the alternatives
 # ---------------------------------------------------------------------------
